@@ -44,12 +44,14 @@
 // The maximum follows lazily: O is rescaled only when a row's maximum rises
 // by more than a number (in log2) that its weights' type has room for, which keeps O's rescaling off the usual path.
 //
-// e4m3 caches stay e4m3 into the tensor core.  Each operand against it is
-// given as a sum of two e4m3 numbers: 4 + 4 significant bits hold a bf16
-// query exactly and a weight to 2^-8, at the rate of one bf16 product and a
-// fourth of the shared memory that widening K and V would take.  A key's
-// scale multiplies its scores; a value's scale, relative to the largest so far,
-// its weight.
+// e4m3 caches stay e4m3 into the tensor core, and each operand against them is
+// given as a sum of 8-bit numbers: a bf16 query as two e4m3 numbers, a weight
+// as three e5m2 numbers, which are the upper bytes of a half-precision number
+// and of what those leave, and so hold eight bits of small weights too.  (One
+// slot may take most of a row's weight and thousands share the rest: with two
+// e4m3 codes weights below 2^-15 of the largest were lost.)  That is a fourth of the
+// shared memory that widening K and V would take.  A key's scale multiplies its
+// scores; a value's scale, relative to the largest so far, its weight.
 //
 // Waits are by an mbarrier's phase parity, which tells the phase waited for only
 // from the one before it.  So whoever waits on a barrier waits for each of its
@@ -68,7 +70,7 @@
 //   64 sequences, 5 tokens each over 500 to 8000, 32 heads of 8, bf16   202 us  5.92 TB/s
 //   2 sequences, 1 token each over 130,000, 64 heads of 8, bf16         175 us  6.11 TB/s
 //     (memory: 87 and 90 % of a copy's rate)
-//   256 sequences, 6 tokens each over 700 to 6000, e4m3                 401 us  4.52 TB/s
+//   256 sequences, 6 tokens each over 700 to 6000, e4m3                 416 us  4.36 TB/s
 //     (the softmax warps' instructions: twice the slots a byte of bf16's)
 //   256 trees of 16 tokens over 100 to 2000, 28 heads of 4, bf16        144 us  4.11 TB/s
 //     (an item's start and end beside eight tiles, and the way from a half's
@@ -107,7 +109,8 @@ constexpr uint32_t kHalfBytes = kTile * 128;  // 128 rows of 128 bytes: one swiz
 constexpr size_t kSmemLimit = 232448;         // 227 KB a CTA
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kNoRow = 0x7fffffff;         // a thread without a row masks nothing
-constexpr int kWideLazyF8 = 4, kNarrowLazyF8 = 5;  // log2 of the largest e4m3 weights
+constexpr int kWideLazyF8 = 4, kNarrowLazyF8 = 6;  // log2 of the largest weights over e4m3,
+constexpr int kTopF8 = 15;                         // and of what they are in their codes
 constexpr float kNone = -1e30f;            // a narrow row's maximum before its first slot
 
 // Workspace: status word, arrival counters [CTA][group] (back to zero after
@@ -150,9 +153,9 @@ struct Item {
 
 struct alignas(16) ScaleStage {  // one tile's scales
   float a[kTile];    // a score's factor: c times the key's scale
-  float w[kTile];    // a weight's factor: the value's scale over 2^(R - 127 + lazy), R the largest so far
+  float w[kTile];    // a weight's factor: the value's scale over 2^(R - 127 + lazy - kTopF8), R the largest so far
   float shift;       // 2^(R of the previous tile - R)
-  float unit;        // 2^(R - 135 + lazy): what O is in units of
+  float unit;        // 2^(R - 127 + lazy - kTopF8): what O is in units of
 };
 struct F8Group {
   ScaleStage sc[kScaleStages];
@@ -173,9 +176,11 @@ struct alignas(16) Rows {
   int vote[2][4];
 };
 // A group's share of the dynamic shared memory, before the ring: queries (two
-// halves of a wide tile, or one of a narrow one and then P), rows, scales.
-constexpr uint32_t kPOff = kHalfBytes, kRowsOff = 2 * kHalfBytes, kF8Off = kRowsOff + 6144, kGroupBytes = 3 * kHalfBytes;
-static_assert(sizeof(Rows) <= 6144 && kF8Off + sizeof(F8Group) <= kGroupBytes, "a group's share");
+// halves of a wide tile, or one of a narrow one and then P's first and last codes),
+// narrow P's middle codes, rows, scales.
+constexpr uint32_t kPOff = kHalfBytes, kMidOff = 2 * kHalfBytes, kRowsOff = kMidOff + kHalfBytes / 2, kF8Off = kRowsOff + 3072,
+                   kGroupBytes = 3 * kHalfBytes;
+static_assert(sizeof(Rows) <= 3072 && kF8Off + sizeof(F8Group) <= kGroupBytes, "a group's share");
 
 struct Group {
   // Its half of the ring holds tiles (of narrow items and pairs) or half tiles (of
@@ -434,30 +439,32 @@ __device__ __forceinline__ void split_e4m3(float a, float b, float c, float d, u
   hi = h0 | h1 << 16;
   lo = e4m3x2_from_f32(a - d0.x, b - d0.y) | e4m3x2_from_f32(c - d1.x, d - d1.y) << 16;
 }
-// The same for weights v in [0, 256], given as v 2^-8, the low codes times kGain.
-// In half precision such a number's bits, cut to the upper 9, are e4m3's code of
-// the nearest number below v (also where that is subnormal); what it leaves is not
-// negative, and is rounded by an integer addition.  Together that is a rounding to
-// at least bf16's 8 bits.  (Rounding the high code too keeps a bit more, and takes a
-// quarter more instructions; conversions to e4m3 take the slow pipe eight cycles a
-// warp.)
+// Four weights as three e5m2 codes each.  e5m2 is half precision's upper byte, so
+// the codes are the upper bytes of the weight in half precision, of what that leaves,
+// and of what that leaves, each remainder held kGain times larger than the one
+// before.  Each code keeps three bits at least, so what is cut off is less than 2^-8
+// of a weight, 0.0003 of it on average (rounding would take two instructions more a
+// pair and code).  The last code's least bit stands for 2^-16 / kGain^2.
 template <int kGain>
-__device__ __forceinline__ void split_weights(float2 a, float2 b, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void split_weights(float2 a, float2 b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
   auto half2 = [](float2 v) {
     uint32_t h;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v.y), "f"(v.x));
     return h;
   };
-  auto left = [](uint32_t x) {  // what the high code leaves: exact
+  auto left = [](uint32_t x) {  // what the code leaves: exact
     uint32_t d;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(x & 0xff80ff80u));
-    if (kGain == 16) asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x4c004c00u));
-    return d + 0x00400040u;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(x & 0xff00ff00u));
+    if (kGain == 8) asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x48004800u));
+    return d;
   };
-  static_assert(kGain == 1 || kGain == 16, "half-precision 16 is 0x4c00; 16 x 16 is e4m3's 256");
-  const uint32_t h0 = half2(a), h1 = half2(b);
-  hi = __byte_perm(h0 >> 7, h1 >> 7, 0x6420);
-  lo = __byte_perm(left(h0) >> 7, left(h1) >> 7, 0x6420);
+  static_assert(kGain == 1 || kGain == 8, "half-precision 8 is 0x4800");
+  uint32_t h0 = half2(a), h1 = half2(b);
+  hi = __byte_perm(h0, h1, 0x7531);
+  h0 = left(h0);
+  h1 = left(h1);
+  mid = __byte_perm(h0, h1, 0x7531);
+  lo = __byte_perm(left(h0), left(h1), 0x7531);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -469,21 +476,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <bool kF8>
 struct Softmax : Role {
   // A raised maximum m is set kHead over the largest score, and raised again when
-  // a score is kLazy over it.  bf16 weights have fp32's range.  An e4m3 weight's
-  // largest code stands for 2^kLazy.  Wide weights sit as high in e4m3's range as
-  // they can, since a low code adds to the same accumulator as its high code and
-  // must not fall below e4m3's least step.  Narrow low codes have columns of their
-  // own and are held kLowGain larger, so there is room to let scores rise by seven:
-  // the error then is 0.00194 of the output, 0.00167 of it the output's own rounding
-  // (256 x 6 tokens; us and error by how far they may rise: 6 507 0.00183, 7 493
-  // 0.00194, 8 481 0.00210, 9 473 0.00238).
+  // a score is kLazy over it.  bf16 weights have fp32's range.  Over e4m3, a weight of
+  // 2^kLazy is 2^kTopF8 in its codes, half precision's largest power of two.  Wide
+  // weights sit as high as they can, since their three codes add to one accumulator
+  // and the last may not fall below e5m2's least step, 2^-16: eight bits are kept of
+  // weights down to 2^-22 of the largest.  Narrow remainders have columns of their own
+  // and are held kGain and kGain^2 larger, so there is room to let scores rise by eight
+  // before a maximum is raised, with eight bits down to 2^-21 of the largest weight (256
+  // x 6 tokens, us by how far they may rise: 7 432, 8 417, 9 407, each a bit of that range).
   static constexpr float kWideLazy = kF8 ? kWideLazyF8 : 16, kNarrowLazy = kNarrowLazyF8;
   static constexpr float kWideHead = kF8 ? -3.f : 0.f, kNarrowHead = 2.f;
-  static constexpr int kLowGain = 16;
+  static constexpr int kGain = 8;
   static constexpr int kJoinRows = kF8 ? 1 : 2;
-  // A wide P's columns: 32 slots are 16 of bf16 pairs, or 8 of high codes and 8 of
-  // low ones 16 columns on
-  static constexpr int kColumns = kF8 ? 8 : 16, kLow = kF8 ? 16 : 8;
+  // A wide P's columns: 32 slots are 16 of bf16 pairs, or 8 of first codes and 8 of
+  // the others 16 and 32 columns on
+  static constexpr int kColumns = kF8 ? 8 : 16, kNext = kF8 ? 16 : 8;
   F8Group &f8;
   Rows &rows;
   uint8_t *p_smem;
@@ -731,7 +738,7 @@ struct Softmax : Role {
     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint32_t hi[8], lo[8];  // P: bf16 pairs in both, or high and low e4m3 codes
+      uint32_t hi[8], mid[8], lo[8];  // P: bf16 pairs in the first two, or the three codes
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
         float2 a =
@@ -745,16 +752,17 @@ struct Softmax : Role {
         sum0 = __fadd2_rn(sum0, a);
         sum1 = __fadd2_rn(sum1, b);
         if (!kF8) {
-          (e < 8 ? hi : lo)[e % 8] = bf16x2_from_f32(a.x, a.y);
-          (e < 8 ? hi : lo)[e % 8 + 1] = bf16x2_from_f32(b.x, b.y);
+          (e < 8 ? hi : mid)[e % 8] = bf16x2_from_f32(a.x, a.y);
+          (e < 8 ? hi : mid)[e % 8 + 1] = bf16x2_from_f32(b.x, b.y);
         } else {
           const float4 w = *reinterpret_cast<const float4 *>(&stage->w[slot0 + 32 * i + 2 * e]);
           split_weights<1>(__fmul2_rn(a, make_float2(w.x, w.y)), __fmul2_rn(b, make_float2(w.z, w.w)), hi[e / 2],
-                           lo[e / 2]);
+                           mid[e / 2], lo[e / 2]);
         }
       }
       tmem_st8(s_buf + kColumns * i, hi);
-      tmem_st8(s_buf + kColumns * i + kLow, lo);
+      tmem_st8(s_buf + kColumns * i + kNext, mid);
+      if (kF8) tmem_st8(s_buf + kColumns * i + 2 * kNext, lo);
     }
     l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
     tmem_wait_st();
@@ -982,7 +990,7 @@ struct Softmax : Role {
           if (!products_done(buf ^ 1)) return false;  // tile t - 1's
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 2 * kNarrow; c += 16) {
+          for (int c = 0; c < 3 * kNarrow; c += 16) {
             uint32_t o[16];
             tmem_ld16(o_at + c, o);
             tmem_wait_ld();
@@ -1004,10 +1012,11 @@ struct Softmax : Role {
         }
       }
       tc_fence_before();
-      // P^T: a slot's 32 weights side by side (high codes, then low ones) in half of a
-      // row of 128 bytes, swizzled as the tensor core reads it
-      uint8_t *dst = p_smem + row * 128;
-      const int sw = (row & 7) ^ (buf * 4);
+      // P^T: a slot's 32 weights side by side (first codes, then last ones) in half of a
+      // row of 128 bytes, swizzled as the tensor core reads it; the middle codes in a
+      // fourth of a row, those of slots 64 on beside those before
+      uint8_t *dst = p_smem + row * 128, *mid_dst = p_smem + (kMidOff - kPOff) + (row & 63) * 128;
+      const int sw = (row & 7) ^ (buf * 4), mid_sw = (row & 7) ^ (buf * 4 + (row >> 6) * 2);
       constexpr int kBlock = 16;  // rows of 16 bytes
 #pragma unroll
       for (int r0 = 0; r0 < kNarrow; r0 += kBlock) {
@@ -1017,13 +1026,14 @@ struct Softmax : Role {
           l[r] = sum.x;
           l[r + 1] = sum.y;
         }
-        uint32_t hi[4], lo[4];
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = r0 + 4 * e;
-          split_weights<kLowGain>(__fmul2_rn(make_float2(y[r], y[r + 1]), make_float2(w, w)),
-                                  __fmul2_rn(make_float2(y[r + 2], y[r + 3]), make_float2(w, w)), hi[e], lo[e]);
+          split_weights<kGain>(__fmul2_rn(make_float2(y[r], y[r + 1]), make_float2(w, w)),
+                               __fmul2_rn(make_float2(y[r + 2], y[r + 3]), make_float2(w, w)), hi[e], mid[e], lo[e]);
         }
+        *reinterpret_cast<uint4 *>(mid_dst + ((r0 / kBlock ^ mid_sw) << 4)) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
         *reinterpret_cast<uint4 *>(dst + (((kNarrow + r0) / kBlock ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         *reinterpret_cast<uint4 *>(dst + ((r0 / kBlock ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       }
@@ -1052,15 +1062,18 @@ struct Softmax : Role {
     if (!join()) return false;
 #pragma unroll 1
     for (int c = 0; c < it.rows; c += 16) {  // O^T: a dimension a thread, so that a row is written side by side
-      uint32_t h[16], lo[16];
+      uint32_t h[16], lo[16], mid[16];
       tmem_ld16(o_at + c, h);
       tmem_ld16(o_at + kNarrow + c, lo);
+      tmem_ld16(o_at + 2 * kNarrow + c, mid);
       tmem_wait_ld();
       pin16(h);
       pin16(lo);
+      pin16(mid);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float o = fmaf(__uint_as_float(lo[e]), 1.f / kLowGain, __uint_as_float(h[e])) * rows.inv[c + e];
+        const float m = fmaf(__uint_as_float(lo[e]), 1.f / kGain, __uint_as_float(mid[e]));
+        const float o = fmaf(m, 1.f / kGain, __uint_as_float(h[e])) * rows.inv[c + e];
         if (c + e < it.rows && row < P.D) {
           if (to_part) __stcg(to_part + 2 * kTile + (size_t)(c + e) * kMaxDim + row, o);
           else P.out[rows.out[c + e] + row] = (uint16_t)bf16x2_from_f32(o, 0.f);
@@ -1105,7 +1118,7 @@ struct Products : Role {
   int ksteps;  // 32 bytes of K each
   uint32_t slot_bytes, s_at, o_at;
   // the descriptors' low words; the high ones are the same for all of them
-  uint32_t q_desc, p_desc, k_desc, v_desc, v_half;
+  uint32_t q_desc, p_desc, mid_desc, k_desc, v_desc, v_half;
   // phases, as bits: p_ready (of either buffer), q_ready (of either place)
   enum : uint32_t { kP0 = 1, kQ0 = 4 };
   uint32_t phases = 0;
@@ -1119,6 +1132,7 @@ struct Products : Role {
     o_at = s_at + kTile;
     q_desc = (uint32_t)smem_desc(smem_addr(smem) + g * kGroupBytes, 16, 1024);
     p_desc = q_desc + (kPOff >> 4);
+    mid_desc = q_desc + (kMidOff >> 4);
     k_desc = (uint32_t)smem_desc(smem_addr(ring), 16, 1024);
     // (V's 128-byte columns lie a half apart)
     v_desc = (uint32_t)smem_desc(smem_addr(ring), kF8 || P.halves == 1 ? 0 : kHalfBytes, 1024);
@@ -1147,8 +1161,10 @@ struct Products : Role {
 
   // S^T = K Q^T and O^T += V^T P^T (e4m3), a step a tile
   __device__ __forceinline__ void narrow_item(const Item &it, int n, int place, Cursor kc, Cursor vc, uint32_t n_items) {
-    constexpr uint32_t id_s = mma_idesc(0, kTile, kNarrow, false, false);
-    constexpr uint32_t id_o = mma_idesc(0, kTile, 2 * kNarrow, true, true);  // (weights' low codes have columns of their own)
+    constexpr uint32_t id_s = mma_idesc(kE4m3, kE4m3, kTile, kNarrow, false, false);
+    // the weights' first and last codes, and their middle ones, in columns of their own
+    constexpr uint32_t id_o = mma_idesc(kE4m3, kE5m2, kTile, 2 * kNarrow, true, true);
+    constexpr uint32_t id_mid = mma_idesc(kE4m3, kE5m2, kTile, kNarrow, true, true);
     constexpr uint32_t q_half = kNarrow * 128 >> 4;
     const uint32_t q_at = q_desc + place * (kHalfBytes / 2 >> 4);
 #pragma unroll 1
@@ -1162,9 +1178,14 @@ struct Products : Role {
         next_phase(&gr.p_ready[buf], kP0 << buf);
         tc_fence_after();
         if (elect_one() && ok) {
-          const uint32_t v = v_desc + (g * P.part + vc.at()) * (slot_bytes >> 4), p = p_desc + buf * (64 >> 4);
+          const uint32_t v = v_desc + (g * P.part + vc.at()) * (slot_bytes >> 4), p = p_desc + buf * (64 >> 4),
+                         mid = mid_desc + buf * (64 >> 4);
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) mma_ss<true>(o_at, v + i * kStepDesc, p + i * kStepDesc, id_o, u > 0 || i > 0);
+          for (int i = 0; i < kSteps; ++i) {
+            mma_ss<true>(o_at, v + i * kStepDesc, p + i * kStepDesc, id_o, u > 0 || i > 0);
+            mma_ss<true>(o_at + 2 * kNarrow, v + i * kStepDesc, mid + (i & 1) * kStepDesc + (i >> 1) * (kNarrow >> 4), id_mid,
+                         u > 0 || i > 0);
+          }
           tc_commit(&gr.empty[vc.at()]);
           tc_commit(&gr.pv_done[buf]);  // last: the CTA may end soon after it
         }
@@ -1195,8 +1216,8 @@ struct Products : Role {
   // half of the ring would hold one tile of each (trees of 16 nodes 165 us by tiles,
   // 152 us by halves; prompts 715 and 737 us).
   __device__ __forceinline__ void wide_item(const Item &it, Cursor kc, Cursor vc, bool pair, uint32_t n_items) {
-    constexpr uint32_t id_s = mma_idesc(kF8 ? 0 : 1, kTile, kTile / 2, false, false);
-    const uint32_t id_o = mma_idesc(kF8 ? 0 : 1, kTile, (uint32_t)P.D, false, true);
+    constexpr uint32_t id_s = mma_idesc(kF8 ? kE4m3 : kBf16, kF8 ? kE4m3 : kBf16, kTile, kTile / 2, false, false);
+    const uint32_t id_o = mma_idesc(kF8 ? kE5m2 : kBf16, kF8 ? kE4m3 : kBf16, kTile, (uint32_t)P.D, false, true);
     constexpr uint32_t kHalf = kHalfBytes >> 4;
     const int steps = __shfl_sync(0xffffffffu, it.steps, 0), by = pair ? 1 : 2;
     const uint32_t size = pair ? P.part : 2 * P.part, unit = pair ? slot_bytes : slot_bytes / 2;
@@ -1228,7 +1249,10 @@ struct Products : Role {
 #pragma unroll
           for (int i = 0; i < kSteps / 2; ++i) {
             mma_ts<kF8>(o_at, p + i * 8, v + i * kStepDesc, id_o, u > 0 || i > 0);
-            if (kF8) mma_ts<kF8>(o_at, p + 16 + i * 8, v + i * kStepDesc, id_o, true);
+            if (kF8) {
+              mma_ts<kF8>(o_at, p + 16 + i * 8, v + i * kStepDesc, id_o, true);
+              mma_ts<kF8>(o_at, p + 32 + i * 8, v + i * kStepDesc, id_o, true);
+            }
           }
           if (last) tc_commit(&v_empty[vc.at()]);
           tc_commit(&gr.pv_done[half]);  // last: the CTA may end soon after it
@@ -1499,7 +1523,7 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
       for (int e = 0; e < 4; ++e) {
         const int kb = ke >> 8 * e & 0xff, vb = ve >> 8 * e & 0xff;
         a[e] = kb ? scale_of_byte(kb) * P.c : 1.f;  // (a masked -inf stays one)
-        const int x = vb - run + 127 - lazy;  // 2^(vb - run - lazy): 2^-8 of codes up to 2^8 for weights up to 2^lazy
+        const int x = vb - run + 127 + kTopF8 - lazy;  // weights up to 2^lazy are up to 2^kTopF8 in their codes
         w[e] = vb && x > 0 ? scale_of_byte(x) : 0.f;
       }
       *reinterpret_cast<float4 *>(&st.a[4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
@@ -1507,7 +1531,7 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
       if (lane == 0) {
         const int d = old - run + 127;
         st.shift = old == 0 ? 1.f : (d > 0 ? scale_of_byte(d) : 0.f);
-        st.unit = ldexpf(1.f, run - 135 + lazy);
+        st.unit = ldexpf(1.f, run - 127 + lazy - kTopF8);
       }
       R.arrive(it.narrow ? &gr.s_full[2 + stage] : &gr.sc_full);
     }

@@ -119,11 +119,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t atom_bytes
 // The high word of every such descriptor with group_bytes 1024.
 constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 
-// Instruction descriptor: fp32 accumulator, A and B of one format (kind::f16: 1
-// = bf16; kind::f8f6f4: 0 = e4m3), M x N, A and B MN-major or K-major.
-__device__ __forceinline__ constexpr uint32_t mma_idesc(uint32_t fmt, uint32_t m, uint32_t n, bool a_mn_major,
-                                                        bool b_mn_major) {
-  return 1u << 4 | fmt << 7 | fmt << 10 | (a_mn_major ? 1u << 15 : 0u) |
+// Instruction descriptor: fp32 accumulator, the formats of A and B (kind::f16:
+// one for both; kind::f8f6f4: each its own), M x N, A and B MN-major or K-major.
+constexpr uint32_t kBf16 = 1, kE4m3 = 0, kE5m2 = 1;
+__device__ __forceinline__ constexpr uint32_t mma_idesc(uint32_t a_fmt, uint32_t b_fmt, uint32_t m, uint32_t n,
+                                                        bool a_mn_major, bool b_mn_major) {
+  return 1u << 4 | a_fmt << 7 | b_fmt << 10 | (a_mn_major ? 1u << 15 : 0u) |
          (b_mn_major ? 1u << 16 : 0u) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
