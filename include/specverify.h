@@ -583,8 +583,10 @@ sv_status_t sv_kv_read(int B, int total, const sv_kv_cache_t *cache, const int32
  * decoding step, K + 1 a verification step, more a piece of a prompt.
  *   dtype        SV_BF16 (q and out); the scores, the softmax and the sums are
  *                fp32, its weights enter the second product in bf16.  SV_E4M3
- *                caches: q enters as a sum of two e4m3 numbers, and a weight,
- *                with its value's power of two, as a sum of three e5m2 numbers,
+ *                caches: q enters as a sum of an e4m3 and an e5m2 number,
+ *                exact for values of at least 2^-14 of their row's largest,
+ *                off by at most 2^-21 of it below, and a weight, with
+ *                its value's power of two, as a sum of three e5m2 numbers,
  *                off by at most 2^-8 of itself, or 2^-29 of the row's largest
  *                weight times the largest power of two where that is more
  *   cache        dim at most 128, strides multiples of 16 bytes

@@ -45,13 +45,14 @@
 // by more than a number (in log2) that its weights' type has room for, which keeps O's rescaling off the usual path.
 //
 // e4m3 caches stay e4m3 into the tensor core, and each operand against them is
-// given as a sum of 8-bit numbers: a bf16 query as two e4m3 numbers, a weight
-// as three e5m2 numbers, which are the upper bytes of a half-precision number
-// and of what those leave, and so hold eight bits of small weights too.  (One
-// slot may take most of a row's weight and thousands share the rest: with two
-// e4m3 codes weights below 2^-15 of the largest were lost.)  That is a fourth of the
-// shared memory that widening K and V would take.  A key's scale multiplies its
-// scores; a value's scale, relative to the largest so far, its weight.
+// given as a sum of 8-bit numbers: a bf16 query as an e4m3 and an e5m2 number,
+// exact down to 2^-14 of its row's largest, a weight as three e5m2 numbers, which are
+// the upper bytes of a half-precision number and of what those leave, and so hold
+// eight bits of small weights too.  (One slot may take most of a row's weight and
+// thousands share the rest: with two e4m3 codes weights below 2^-15 of the
+// largest were lost.)  That is a fourth of the shared memory that widening K and V
+// would take.  A key's scale multiplies its scores; a value's scale, relative to the
+// largest so far, its weight.
 //
 // Waits are by an mbarrier's phase parity, which tells the phase waited for only
 // from the one before it.  So whoever waits on a barrier waits for each of its
@@ -431,13 +432,15 @@ __device__ __forceinline__ float q_scale(uint32_t top_bits, float &inv) {
   inv = top_bits < 0x7f800000u ? scale_of_byte(254 - byte) : __uint_as_float(0x7fc00000u);
   return scale_of_byte(byte);
 }
-// Four values as e4m3 codes and the codes of what those leave.
-__device__ __forceinline__ void split_e4m3(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo) {
+// Four values as e4m3 codes and the e5m2 codes of what those leave.  An e4m3 code
+// leaves at most 8 units of a bf16 value's last place, which e5m2's three bits hold
+// exactly, whatever their size; e4m3 would hold them down to 2^-9 only.
+__device__ __forceinline__ void split_queries(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo) {
   const uint32_t h0 = e4m3x2_from_f32(a, b), h1 = e4m3x2_from_f32(c, d);
   const float2 d0 = f32x2_from_f16x2(f16x2_from_e4m3x2((uint16_t)h0));
   const float2 d1 = f32x2_from_f16x2(f16x2_from_e4m3x2((uint16_t)h1));
   hi = h0 | h1 << 16;
-  lo = e4m3x2_from_f32(a - d0.x, b - d0.y) | e4m3x2_from_f32(c - d1.x, d - d1.y) << 16;
+  lo = e5m2x2_from_f32(a - d0.x, b - d0.y) | e5m2x2_from_f32(c - d1.x, d - d1.y) << 16;
 }
 // Four weights as three e5m2 codes each.  e5m2 is half precision's upper byte, so
 // the codes are the upper bytes of the weight in half precision, of what that leaves,
@@ -1162,6 +1165,7 @@ struct Products : Role {
   // S^T = K Q^T and O^T += V^T P^T (e4m3), a step a tile
   __device__ __forceinline__ void narrow_item(const Item &it, int n, int place, Cursor kc, Cursor vc, uint32_t n_items) {
     constexpr uint32_t id_s = mma_idesc(kE4m3, kE4m3, kTile, kNarrow, false, false);
+    constexpr uint32_t id_low = mma_idesc(kE4m3, kE5m2, kTile, kNarrow, false, false);
     // the weights' first and last codes, and their middle ones, in columns of their own
     constexpr uint32_t id_o = mma_idesc(kE4m3, kE5m2, kTile, 2 * kNarrow, true, true);
     constexpr uint32_t id_mid = mma_idesc(kE4m3, kE5m2, kTile, kNarrow, true, true);
@@ -1200,7 +1204,7 @@ struct Products : Role {
         for (int i = 0; i < 4; ++i) {
           if (!kFull && i >= ksteps) break;
           mma_ss<true>(s_to, k + i * 2, q_at + i * 2, id_s, i > 0);
-          mma_ss<true>(s_to, k + i * 2, q_at + q_half + i * 2, id_s, true);
+          mma_ss<true>(s_to, k + i * 2, q_at + q_half + i * 2, id_low, true);
         }
         tc_commit(&gr.s_full[2 + buf]);
         tc_commit(&gr.empty[kc.at()]);
@@ -1217,6 +1221,7 @@ struct Products : Role {
   // 152 us by halves; prompts 715 and 737 us).
   __device__ __forceinline__ void wide_item(const Item &it, Cursor kc, Cursor vc, bool pair, uint32_t n_items) {
     constexpr uint32_t id_s = mma_idesc(kF8 ? kE4m3 : kBf16, kF8 ? kE4m3 : kBf16, kTile, kTile / 2, false, false);
+    constexpr uint32_t id_low = mma_idesc(kE5m2, kE4m3, kTile, kTile / 2, false, false);
     const uint32_t id_o = mma_idesc(kF8 ? kE5m2 : kBf16, kF8 ? kE4m3 : kBf16, kTile, (uint32_t)P.D, false, true);
     constexpr uint32_t kHalf = kHalfBytes >> 4;
     const int steps = __shfl_sync(0xffffffffu, it.steps, 0), by = pair ? 1 : 2;
@@ -1271,7 +1276,7 @@ struct Products : Role {
           const uint32_t oq = kF8 ? i * 2 : (i >> 2) * kHalf + (i & 3) * 2;
           const uint32_t ok = kF8 ? i * 2 : (i >> 2) * halves_k + (i & 3) * 2;
           mma_ss<kF8>(s_to, q_desc + oq, k + ok, id_s, i > 0);
-          if (kF8) mma_ss<kF8>(s_to, q_desc + kHalf + oq, k + ok, id_s, true);
+          if (kF8) mma_ss<kF8>(s_to, q_desc + kHalf + oq, k + ok, id_low, true);
         }
         tc_commit(&gr.s_full[half]);
         if (last) tc_commit(&k_empty[kc.at()]);
@@ -1572,7 +1577,7 @@ __device__ __forceinline__ void copy_queries(const AttParams &P, const Item &it,
   for (int r = rows + lane / per; it.narrow && r < kNarrow; r += step) *reinterpret_cast<uint4 *>(place(r)) = make_uint4(0, 0, 0, 0);
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
-// What the products need of them: a negative scale's sign, or the two e4m3 codes.
+// What the products need of them: a negative scale's sign, or the two codes.
 template <bool kF8>
 __device__ __forceinline__ void make_queries(const AttParams &P, const Item &it, int lane, float *scales, uint8_t *tile) {
   const uint32_t half = it.narrow ? kNarrow * 128 : kHalfBytes;
@@ -1606,7 +1611,7 @@ __device__ __forceinline__ void make_queries(const AttParams &P, const Item &it,
       float inv;
       const float s = q_scale(top << 16, inv);
       uint32_t hi, lo;
-      split_e4m3(bf16lo(x.x) * inv, bf16hi(x.x) * inv, bf16lo(x.y) * inv, bf16hi(x.y) * inv, hi, lo);
+      split_queries(bf16lo(x.x) * inv, bf16hi(x.x) * inv, bf16lo(x.y) * inv, bf16hi(x.y) * inv, hi, lo);
       uint8_t *dst = tile + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
       *reinterpret_cast<uint32_t *>(dst) = hi;
       *reinterpret_cast<uint32_t *>(dst + half) = lo;

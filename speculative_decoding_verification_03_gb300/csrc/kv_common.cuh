@@ -40,11 +40,16 @@ __device__ __forceinline__ int tree_parent(const int32_t *parents, int tree_node
   return p;
 }
 
-// Two fp32 values to two e4m3 codes (nearest even, saturating), `lo` in the
+// Two fp32 values to two e4m3 or e5m2 codes (nearest even, saturating), `lo` in the
 // low byte, and e4m3 pairs widened to half pairs (exact).
 __device__ __forceinline__ uint32_t e4m3x2_from_f32(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint16_t c) {

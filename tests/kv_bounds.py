@@ -64,9 +64,9 @@ class Sink:
         assert binding.status(ws) == (0, 0)
         want, mag, terms, wl = self.exact()
         # A score is a sum of D products in fp32 (D roundings of at most 2^-24 of the
-        # terms' sum, 4 more for scaling and exponent) over queries within 2^-18 of
+        # terms' sum, 4 more for scaling and exponent) over queries within 2^-21 of
         # their row's largest; a weight is off by 2^-8 of it, the output is rounded to bf16.
-        ds = (self.D + 4) * 2.0 ** -24 * terms + 2.0 ** -21 + 2.0 ** -18 * terms
+        ds = (self.D + 4) * 2.0 ** -24 * terms + 2.0 ** -21 + 2.0 ** -21 * terms
         tol = (2.0 ** -8 + 2 * ds + 2.0 ** -18)[..., None] * mag + 2.0 ** -8 * np.abs(want)
         got = out.cpu().double().numpy().reshape((self.batch,) + want.shape)
         gl = lse.cpu().double().numpy().reshape((self.batch,) + wl.shape)
