@@ -52,7 +52,7 @@
 // thousands share the rest: with two e4m3 codes weights below 2^-15 of the
 // largest were lost.)  That is a fourth of the shared memory that widening K and V
 // would take.  A key's scale multiplies its scores; a value's scale, relative to the
-// largest so far, its weight.
+// largest of late, its weight.
 //
 // Waits are by an mbarrier's phase parity, which tells the phase waited for only
 // from the one before it.  So whoever waits on a barrier waits for each of its
@@ -112,6 +112,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kNoRow = 0x7fffffff;         // a thread without a row masks nothing
 constexpr int kWideLazyF8 = 4, kNarrowLazyF8 = 6;  // log2 of the largest weights over e4m3,
 constexpr int kTopF8 = 15;                         // and of what they are in their codes
+constexpr int kScaleDrop = 4, kScaleFall = 60;     // log2: see scales()
 constexpr float kNone = -1e30f;            // a narrow row's maximum before its first slot
 
 // Workspace: status word, arrival counters [CTA][group] (back to zero after
@@ -154,7 +155,7 @@ struct Item {
 
 struct alignas(16) ScaleStage {  // one tile's scales
   float a[kTile];    // a score's factor: c times the key's scale
-  float w[kTile];    // a weight's factor: the value's scale over 2^(R - 127 + lazy - kTopF8), R the largest so far
+  float w[kTile];    // a weight's factor: the value's scale over 2^(R - 127 + lazy - kTopF8), R the largest of late
   float shift;       // 2^(R of the previous tile - R)
   float unit;        // 2^(R - 127 + lazy - kTopF8): what O is in units of
 };
@@ -1498,7 +1499,7 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
     const Item &it = *item_at;
     const int n = it.n;
     const int lazy = it.narrow ? kNarrowLazyF8 : kWideLazyF8;
-    int run = 0;  // the largest value exponent so far
+    int run = 0;  // R, the largest value exponent of late
     for (int t = 0; t < n; ++t) {
 #pragma unroll 1
       for (int tries = under_way ? 1 : kScaleAhead; tries > 0; --tries) fetch();
@@ -1516,8 +1517,12 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
       int top = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, (int)(ve >> 8 * e & 0xff));
+      // R rises at once, and falls when a tile's largest is more than kScaleDrop below
+      // it, so that one large value costs the weights of its own tile's slots at most.  (O
+      // has room for kScaleFall: it is below 2^56.)
       const int old = run;
-      run = max(old, __reduce_max_sync(0xffffffffu, top));
+      run = __reduce_max_sync(0xffffffffu, top);
+      if (run < old) run = run < old - kScaleDrop ? max(run, old - kScaleFall) : old;
       // a narrow tile's scales go by its scores' buffer and are announced with them
       const int stage = it.narrow ? t & 1 : 0;
       ScaleStage &st = f8.sc[stage];
