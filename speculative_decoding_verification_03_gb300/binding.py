@@ -7,6 +7,7 @@ is not a GB300 (sm_103), the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -148,6 +149,16 @@ def _stream(stream):
     if stream is None:  # the current stream, without a Stream object (which takes longer than a small kernel)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _made_on(stream):
+    """Where a call allocates what it was not given: memory of the stream that it runs
+    on.  Memory of another stream may still be in use there, and may be given
+    away there, once dropped, while the call is under way."""
+    return _HERE_ALREADY if stream is None else torch.cuda.stream(stream)
 
 
 def _check(rc, where):
@@ -546,7 +557,8 @@ def rope(x, positions, plan: RopePlan, inverse: bool = False, out=None, stream=N
     if positions.shape != (T,):
         raise ValueError("positions must be [tokens]")
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        with _made_on(stream):
+            out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
     elif _heads(out, "out", x.dtype).shape != x.shape:
         raise ValueError("out must have x's shape")
     rc = lib().sv_rope(T, H, D, code, x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(),
@@ -573,7 +585,8 @@ def kv_append(cache: KVCache, k, v, q_start, kv_len, block_table, q=None, plan: 
         if q.shape != (T, Hq, cache.dim):
             raise ValueError("q must be [tokens][heads][cache dim]")
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.dim), dtype=q.dtype, device=q.device)
+            with _made_on(stream):
+                q_out = torch.empty((T, Hq, cache.dim), dtype=q.dtype, device=q.device)
         elif _heads(q_out, "q_out", q.dtype).shape != q.shape:
             raise ValueError("q_out must have q's shape")
         qp, qs, op, os_ = q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
@@ -602,10 +615,11 @@ def kv_read(cache: KVCache, kv_start, block_table, total: int, dtype=torch.bfloa
     if B < 0 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("kv_start must be [B + 1] and block_table [B][pages]")
     shape = (int(total), cache.heads, cache.dim)
-    if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=kv_start.device)
-    if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=kv_start.device)
+    with _made_on(stream):
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=dtype, device=kv_start.device)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=dtype, device=kv_start.device)
     for t in (out_k, out_v):
         if _dev(t, "out_k and out_v", dtype).shape != shape:
             raise ValueError("out_k and out_v must be [total][heads][dim]")
@@ -619,8 +633,9 @@ def kv_read(cache: KVCache, kv_start, block_table, total: int, dtype=torch.bfloa
 
 def attention_workspace(device=None, stream=None):
     """A workspace for paged_attention, cleared (sv_attention_reset)."""
-    ws = torch.empty(int(lib().sv_attention_workspace_bytes()), dtype=torch.uint8,
-                     device=device if device is not None else "cuda")
+    with _made_on(stream):
+        ws = torch.empty(int(lib().sv_attention_workspace_bytes()), dtype=torch.uint8,
+                         device=device if device is not None else "cuda")
     _check(lib().sv_attention_reset(_ptr(ws), ws.numel(), _stream(stream)), "sv_attention_reset")
     return ws
 
@@ -629,21 +644,23 @@ def paged_attention(q, cache: KVCache, q_start, kv_len, block_table, parents=Non
                     out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
     """sv_paged_attention: (out [tokens][heads][dim] bfloat16, lse [tokens][heads]
     float32 or None).  scale is 1 / sqrt(dim) when not given; `workspace`
-    (attention_workspace()) is made per call when not given."""
+    (attention_workspace()) is made per call when not given, and then the call's
+    status cannot be read.  With `stream`, what is not given is allocated on it."""
     _heads(q, "q", torch.bfloat16)
     B = _batch(q_start, kv_len, block_table, parents)
     T, Hq, D = q.shape
     if D != cache.dim:
         raise ValueError("q must be [tokens][heads][cache dim]")
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif _heads(out, "out", q.dtype).shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    elif _dev(lse, "lse", torch.float32).shape != (T, Hq):
-        raise ValueError("lse must be [tokens][heads]")
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        elif _heads(out, "out", q.dtype).shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if lse is None:
+            if want_lse:
+                lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        elif _dev(lse, "lse", torch.float32).shape != (T, Hq):
+            raise ValueError("lse must be [tokens][heads]")
     if workspace is None:
         workspace = attention_workspace(q.device, stream)
     rc = lib().sv_paged_attention(B, T, Hq, cache.ref, SV_BF16, q.data_ptr(), q.stride(0), q.stride(1),
