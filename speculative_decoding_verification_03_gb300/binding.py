@@ -663,6 +663,7 @@ def paged_attention(q, cache: KVCache, q_start, kv_len, block_table, parents=Non
             raise ValueError("lse must be [tokens][heads]")
     if workspace is None:
         workspace = attention_workspace(q.device, stream)
+    _dev(workspace, "workspace", torch.uint8)
     rc = lib().sv_paged_attention(B, T, Hq, cache.ref, SV_BF16, q.data_ptr(), q.stride(0), q.stride(1),
                                   q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
                                   _ptr(parents), 0 if parents is None else parents.shape[1],
