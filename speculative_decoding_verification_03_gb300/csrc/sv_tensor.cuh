@@ -1,7 +1,8 @@
 // Blackwell tensor-core building blocks as inline PTX: tensor memory (TMEM)
 // allocation, loads and stores, tcgen05.mma descriptors and issue, and tiled
-// TMA copies.  One CTA (cta_group::1); every wait is a bounded mbarrier wait
-// (sv_device.cuh).
+// TMA copies.  One CTA (cta_group::1).  Nothing here waits without an end but for
+// tcgen05.wait and cp.async.wait, which end with the work that was issued; mbarrier
+// waits are sv_device.cuh's, limited in time or by whoever uses them.
 #pragma once
 
 #include <cuda.h>
@@ -60,14 +61,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
                : "r"(taddr)
                : "memory");
 }
-// 8 columns of registers, or of zeros.
+// 8 columns of registers.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
-}
-__device__ __forceinline__ void tmem_zero8(uint32_t taddr) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr), "r"(0) : "memory");
 }
 // Keep uses of a load's registers behind the wait (the compiler sees plain
 // registers that the load has already written).
