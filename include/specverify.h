@@ -58,7 +58,8 @@ typedef enum {
     SV_ERR_TOKEN_RANGE = 5,  /* device: a drafted token outside [0, V)          */
     SV_ERR_TIMEOUT = 6,      /* device: a bounded wait gave up                  */
     SV_ERR_WORKSPACE = 7,    /* workspace (or AV state) too small or misaligned */
-    SV_ERR_BAD_LEN = 8,      /* device: draft_len[b] outside [0, K]             */
+    SV_ERR_BAD_LEN = 8,      /* device: draft_len[b] outside [0, K]; attention:
+                                kv_len[b] or parents (SV_FLAG_BAD_LEN there)    */
     SV_ERR_BAD_TEMP = 9,     /* device: temperature[b] negative or NaN          */
     SV_ERR_PAGE_RANGE = 10   /* device: a page index outside the cache          */
 } sv_status_t;

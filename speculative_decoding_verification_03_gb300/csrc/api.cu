@@ -569,7 +569,7 @@ const char *sv_strerror(sv_status_t s) {
     case SV_ERR_TOKEN_RANGE: return "drafted token out of range";
     case SV_ERR_TIMEOUT: return "device wait timed out";
     case SV_ERR_WORKSPACE: return "workspace too small or misaligned";
-    case SV_ERR_BAD_LEN: return "draft_len outside [0, K]";
+    case SV_ERR_BAD_LEN: return "length out of range (draft_len outside [0, K], kv_len outside its pages) or malformed token tree";
     case SV_ERR_BAD_TEMP: return "negative or NaN temperature";
     case SV_ERR_PAGE_RANGE: return "page index outside the cache";
   }
