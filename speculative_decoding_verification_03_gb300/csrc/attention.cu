@@ -11,7 +11,7 @@
 //           products are turned round, S^T = K Q^T and O^T = V^T P^T, with the tile's
 //           128 slots (then the 128 dimensions) as M and 32 rows as N.  One thread
 //           takes one slot of all rows, so all 128 share what e4m3 weights cost
-//           (256 x 6 tokens 398 us, as wide items 726; in bf16 wide items do as well
+//           (256 x 6 tokens 402 us, as wide items 717; in bf16 wide items do as well
 //           or better: 64 x 5 tokens over 300 32 us and narrow ones 39, over 500 to
 //           8000 201 and 199, 256 x 1 over 400 90 and 91, 1 over 1021 15 and 16)
 //   wide    up to 128 rows: S = Q K^T, O = P V by half tiles of 64 slots, one thread
@@ -66,19 +66,24 @@
 // time).  Hence loops are rolled where registers allow, each step has one site,
 // and a wait is a few instructions.
 //
-// Measured (one GB300; copy 6779 GB/s, bf16 products 1928 TFLOP/s), the bytes or
-// operations that the method cannot do without over the time:
+// Measured (one GB300; copy 6779 GB/s, bf16 products 1928 TFLOP/s; in a graph), the
+// bytes or operations that the method cannot do without over the time.  (These are the
+// kernel's as it is.  Figures beside a choice compare what was tried with it; those
+// for forms that are gone are from when they were tried.)
 //   64 sequences, 5 tokens each over 500 to 8000, 32 heads of 8, bf16   202 us  5.92 TB/s
-//   2 sequences, 1 token each over 130,000, 64 heads of 8, bf16         175 us  6.11 TB/s
+//   2 sequences, 1 token each over 130,000, 64 heads of 8, bf16         174 us  6.14 TB/s
 //     (memory: 87 and 90 % of a copy's rate)
-//   256 sequences, 6 tokens each over 700 to 6000, e4m3                 416 us  4.36 TB/s
+//   256 sequences, 6 tokens each over 700 to 6000, e4m3                 402 us  4.50 TB/s
 //     (the softmax warps' instructions: twice the slots a byte of bf16's)
 //   256 trees of 16 tokens over 100 to 2000, 28 heads of 4, bf16        144 us  4.11 TB/s
 //     (an item's start and end beside eight tiles, and the way from a half's
 //     weights over its products to the scores after it)
-//   3 prompts of 1500 to 2048 tokens over 3000 to 16000, bf16           687 us  1233 TFLOP/s
+//   3 prompts of 1500 to 2048 tokens over 3000 to 16000, bf16           690 us  1228 TFLOP/s
 //     (the same way, and shared memory's feed of the scores' products: with half
-//     of those 623 us)
+//     of those 623 us; 712 us over seconds, when the power limit lowers the clock)
+//   the trees and the prompts over e4m3                                 272 and 1439 us
+//     (wide items: five products for two, three codes a weight, a maximum that may
+//     rise by one)
 //   1 token over 1021, 32 heads of 8, bf16                               16 us
 //     (latency: lengths, items, queries, one tile, eight parts joined)
 #include <cmath>
@@ -102,8 +107,8 @@ constexpr int kScaleStages = 2;            // (a wide item uses one)
 constexpr int kScaleAhead = 8;             // tiles whose scale bytes are under way
 // What an item's start and end take, in tile steps: by the kind of item, as short
 // tiles leave them more.  Measured, us: bf16 single items with 2 / 3 / 4, trees of 16
-// nodes 148 / 151 / 154, 64 x 5 tokens 194 / 194 / 195; e4m3 with 4 / 6 / 8, 256 x 6
-// tokens 441 / 435 / 425; pairs with 5 / 6 / 8, prompts 711 / 715 / 720.
+// nodes 144 / 146 / 147, 64 x 5 tokens 202 / 202 / 203; e4m3 with 4 / 6 / 8 / 10, 256 x 6
+// tokens 427 / 410 / 402 / 407; pairs with 5 / 6 / 8, prompts 690 / 691 / 700.
 constexpr int kItemUnits = 2, kItemUnitsF8 = 8, kItemUnitsPair = 5;
 constexpr int kNarrow = 32;                // rows of a narrow tile
 constexpr uint32_t kHalfBytes = kTile * 128;  // 128 rows of 128 bytes: one swizzled half of a tile
@@ -503,7 +508,7 @@ struct Softmax : Role {
   // weights down to 2^-22 of the largest.  Narrow remainders have columns of their own
   // and are held kGain and kGain^2 larger, so there is room to let scores rise by eight
   // before a maximum is raised, with eight bits down to 2^-21 of the largest weight (256
-  // x 6 tokens, us by how far they may rise: 7 432, 8 417, 9 407, each a bit of that range).
+  // x 6 tokens, us by how far they may rise: 7 413, 8 402, 9 393, each a bit of that range).
   static constexpr float kWideLazy = kF8 ? kWideLazyF8 : 16, kNarrowLazy = kNarrowLazyF8;
   static constexpr float kWideHead = kF8 ? -3.f : 0.f, kNarrowHead = 2.f;
   static constexpr int kGain = 8;
@@ -555,7 +560,7 @@ struct Softmax : Role {
   // and sums, a row a thread, then each warp adds up rows, four columns a lane;
   // both with eight parts' loads under way, of two rows with bf16 caches (1 x 32
   // tokens over 4000 55 -> 48 us; with e4m3 the registers are missed in the loops
-  // over tiles: 256 x 6 tokens 390 -> 561 us).
+  // over tiles: 256 x 6 tokens 402 -> 564 us).
   __device__ __forceinline__ bool join_parts(const Item &it) {
     __threadfence();
     if (!join()) return false;
@@ -1129,7 +1134,7 @@ struct Softmax : Role {
 
 // ---- the products ----------------------------------------------------------------------
 // kFull: heads of kMaxDim values, whose products' steps over them need no test (256 x 6
-// tokens 397 us with it, 412 without; prompts 692 and 705).
+// tokens 402 us with it, 413 without; prompts 690 and 698).
 template <bool kF8, bool kFull>
 struct Products : Role {
   static constexpr int kSteps = kF8 ? 4 : 8;  // of 32 or 16 slots in a tile
@@ -1828,8 +1833,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // 128 registers a thread at launch (65,536 over 512 threads), shared out
   // again by warpgroup: 2 x 168 + 2 x 88 = 2 x 184 + 2 x 72 = 4 x 128.  Measured with
-  // 168 / 176 / 184 for the softmax warps, us: 256 x 6 e4m3 tokens 401 / 411 / 430, bf16
-  // trees of 16 nodes 148 / 145 / 143, 64 x 5 bf16 tokens 200 / 197 / 197.
+  // 168 / 176 / 184 for the softmax warps, us: 256 x 6 e4m3 tokens 402 / 412 / 417, bf16
+  // trees of 16 nodes 148 / 144 / 144, 64 x 5 bf16 tokens 204 / 202 / 202.
   if (warp < 8) {
     const int g = warp >> 2;
     uint8_t *mine = smem + g * kGroupBytes;
