@@ -590,7 +590,8 @@ sv_status_t sv_kv_read(int B, int total, const sv_kv_cache_t *cache, const int32
  *                its value's power of two, as a sum of three e5m2 numbers,
  *                off by at most 2^-8 of itself, or 2^-25 of the row's largest
  *                weight times the largest power of two among the 128 slots that
- *                it lies with (j / 128), where that is more
+ *                it lies with (j / 128), or 2^-60 times the sequence's
+ *                largest, where that is more
  *   cache        dim at most 128, strides multiples of 16 bytes
  *   q, out       device [T][q_heads][dim], 16-byte aligned, strides in elements,
  *                multiples of 8; q_heads a multiple of cache->heads, at most

@@ -1520,7 +1520,7 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
     const Item &it = *item_at;
     const int n = it.n;
     const int lazy = it.narrow ? kNarrowLazyF8 : kWideLazyF8;
-    int run = 0;  // R, the largest value exponent of late
+    int run = 0, most = 0;  // R, the largest value exponent of late, and of all the item's
     for (int t = 0; t < n; ++t) {
 #pragma unroll 1
       for (int tries = under_way ? 1 : kScaleAhead; tries > 0; --tries) fetch();
@@ -1535,15 +1535,16 @@ __device__ void scales(const AttParams &P, Shared &sh, int g, F8Group &f8) {
         ke = left <= 0 ? 0 : ke & ((1u << 8 * left) - 1u);
         ve = left <= 0 ? 0 : ve & ((1u << 8 * left) - 1u);
       }
-      int top = 0;
+      int top = 1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, (int)(ve >> 8 * e & 0xff));
       // R rises at once, and falls when a tile's largest is more than kScaleDrop below
       // it, so that one large value costs the weights of its own tile's slots at most.  (O
-      // has room for kScaleFall: it is below 2^56.)
+      // is below 2^56 when it comes in, and grows as R falls: kScaleFall leaves it in range.)
       const int old = run;
       run = __reduce_max_sync(0xffffffffu, top);
-      if (run < old) run = run < old - kScaleDrop ? max(run, old - kScaleFall) : old;
+      most = max(most, run);
+      if (run < old) run = run < old - kScaleDrop ? max(run, most - kScaleFall) : old;
       // a narrow tile's scales go by its scores' buffer and are announced with them
       const int stage = it.narrow ? t & 1 : 0;
       ScaleStage &st = f8.sc[stage];

@@ -94,3 +94,13 @@ def test_scales_that_fall_and_rise(tokens):
     scaled(c, [j for j in range(3000) if j // 128 % 3 == 1], 20)
     scaled(c, [j for j in range(3000) if j // 128 % 3 == 2], -20)
     check(c)
+
+
+@pytest.mark.parametrize("first", [100, 40])
+@pytest.mark.parametrize("tokens", [5, 25, 50])
+def test_scales_that_fall_far(tokens, first):
+    """Values fall by 2^50 a tile, three times: the largest stay what they are."""
+    c = ref.Case([600], [tokens], 4, 1, 64, 16, True, seed=tokens)
+    for t in range(5):
+        scaled(c, range(128 * t, min(128 * (t + 1), 600)), max(first - 50 * t, first - 150))
+    check(c)
