@@ -1359,8 +1359,9 @@ struct Products : Role {
     fence_async_smem();
     __syncwarp();
   }
-  // Tensor and shared memory go only once the products under way are done; on
-  // the usual path the softmax warps have seen to that.
+  // Tensor and shared memory go only once the products under way are done, and a
+  // copy of queries that another group's time-out left under way; on the usual path the
+  // softmax warps, and who waits for the queries, have seen to that.
   __device__ void fail() {
     const uint64_t t0 = global_ns();
     while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
